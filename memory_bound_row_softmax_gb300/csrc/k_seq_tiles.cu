@@ -153,7 +153,10 @@ __device__ __forceinline__ Unit make_unit(const TilesParams &p, const Sequence &
 // (`sw`: its place in the swizzle atom): x * 0 summed is NaN once one of them is
 // infinite or NaN.  Such values are set to zero, the key's bit in the tile's mask
 // `bad` first: whoever finds the zero finds the bit.  Rows past the last key
-// (leftovers in shared memory) get no bit.
+// (leftovers in shared memory) get no bit.  The fence comes last on every path, before
+// the group lets its product read the tile: the other group looks at the same tile, so
+// a thread that finds nothing bad may have found that group's zeros, which the product
+// (async proxy) is sure to read only past a fence of this thread's.
 template <typename T, int D>
 __device__ __forceinline__ void zero_bad_values(uint8_t *v, int sw, uint32_t *bad, int r, bool real) {
     constexpr uint32_t kHalf = Layout<D>::kHalf;
@@ -164,17 +167,19 @@ __device__ __forceinline__ void zero_bad_values(uint8_t *v, int sw, uint32_t *ba
         acc[0] = add_times_zero<T>(add_times_zero<T>(acc[0], w.x), w.y);
         acc[1] = add_times_zero<T>(add_times_zero<T>(acc[1], w.z), w.w);
     }
-    if (!((acc[0] | acc[1]) & 0x7fff7fffu)) return;
-    if (real) {
-        atomicOr(bad + (r >> 5), 1u << (r & 31));
-        __threadfence_block();
-    }
+    if ((acc[0] | acc[1]) & 0x7fff7fffu) {
+        if (real) {
+            atomicOr(bad + (r >> 5), 1u << (r & 31));
+            __threadfence_block();
+        }
 #pragma unroll 1
-    for (int c = 0; c < D / 8; ++c) {
-        uint4 *const w = reinterpret_cast<uint4 *>(v + (c >> 3) * kHalf + (((c & 7) ^ sw) << 4));
-        *w = make_uint4(finite_or_zero<T>(w->x), finite_or_zero<T>(w->y), finite_or_zero<T>(w->z), finite_or_zero<T>(w->w));
+        for (int c = 0; c < D / 8; ++c) {
+            uint4 *const w = reinterpret_cast<uint4 *>(v + (c >> 3) * kHalf + (((c & 7) ^ sw) << 4));
+            *w = make_uint4(finite_or_zero<T>(w->x), finite_or_zero<T>(w->y), finite_or_zero<T>(w->z),
+                            finite_or_zero<T>(w->w));
+        }
     }
-    mbrs::fence_proxy_async_smem();  // before the product reads the tile
+    mbrs::fence_proxy_async_smem();
 }
 
 // The values set to zero, added back to a row that keeps their keys [from, upto),
