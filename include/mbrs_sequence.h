@@ -21,7 +21,8 @@
  *
  * A query that keeps no key gets o = 0 and lse = -inf.  Keys outside the kept
  * ones never reach a query's result, whatever their bits are (values that are
- * infinite or NaN included).
+ * infinite or NaN included).  An infinite or NaN value of a key that is kept makes
+ * its element of the result infinite or NaN, however small the key's weight.
  *
  * The cache.  k and v are arrays of pages: element (page, slot, head, d) lies
  * at page * page_stride + slot * token_stride + head * head_stride + d, so both

@@ -437,11 +437,11 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
+                // a weight of zero too: infinite and NaN values of keys that the row keeps
+                // reach it (a warp whose keys it does not keep holds zeros)
                 const float4 v = *reinterpret_cast<const float4 *>(merge + (w * 16 + r) * L::kColPitch + c4);
-                if (weight[w] != 0.f) {  // a warp without keys may hold anything times zero
-                    acc.x += v.x * weight[w], acc.y += v.y * weight[w];
-                    acc.z += v.z * weight[w], acc.w += v.w * weight[w];
-                }
+                acc.x += v.x * weight[w], acc.y += v.y * weight[w];
+                acc.z += v.z * weight[w], acc.w += v.w * weight[w];
             }
             if (r < rows && ok) {
                 if (whole) {
@@ -516,8 +516,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_rows_join(const __grid_cons
             if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
             else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (w != 0.f) acc[e] += v[e] * w;
+            for (int e = 0; e < V; ++e) acc[e] += v[e] * w;
         }
         __syncthreads();  // the previous row's sums have been read
 #pragma unroll

@@ -853,7 +853,9 @@ __global__ void __launch_bounds__(kTile) k_tiles_join(const __grid_constant__ Ti
     for (int b = first; b <= last; ++b) {
         const float2 st = state(b);
         const float w = ex2(st.x - safe_shift(shift));
-        if (w == 0.f && !isnan(st.y)) continue;  // a part without keys has no O
+        // a part without keys has no O; one far below the others has, and its infinite
+        // and NaN values reach the row
+        if (st.x == -INFINITY && st.y == 0.f) continue;
         all += st.y * w;
         const float *o = p.parts + (((int64_t)(2 * b + (b == first ? 1 : 0)) * 2 + t) * (D / 4) * kTile + r) * 4;
 #pragma unroll
