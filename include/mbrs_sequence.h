@@ -43,8 +43,9 @@
  * Types: SOFTMAX_F16 or SOFTMAX_BF16; head_dim 64 or 128; heads a multiple of
  * kv_heads, at most 128 query heads to one key/value head; page_size a multiple
  * of 8.  Arithmetic: products of the 16-bit inputs accumulated in fp32, exp in
- * fp32, the probabilities rounded to the input type for the second product, o
- * accumulated in fp32, divided by the fp32 normaliser and rounded once.
+ * fp32, the probabilities rounded to the input type for the second product (in
+ * fp16 with all its bits down to 2^-21 of a row's largest, and none below 2^-32),
+ * o accumulated in fp32, divided by the fp32 normaliser and rounded once.
  *
  * Ownership: the caller owns every buffer and the stream.  The calls are
  * asynchronous on `stream`, allocate nothing on the device, keep nothing from

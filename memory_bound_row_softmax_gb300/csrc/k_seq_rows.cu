@@ -13,13 +13,13 @@
 // Work split: the work of all items, in the order (sequence, row block, kv head),
 // is cut into equal stretches, one per block, whatever the sequences' lengths.  Each block finds its stretch from q_starts and kv_lens
 // itself (one scan over the batch).  A block walks its stretch item by item; an
-// item it holds whole is finished there, of a cut one the part's (max, sum, O)
+// item it holds whole is finished there, of a cut one the part's (shift, sum, O)
 // goes to the workspace in fp32 and k_rows_join merges the parts in order
 // (the merge rule of common.cuh), so results do not depend on timing.
 //
 // Roles: the last warp feeds a ring of K/V tiles with TMA (one lane per copy: a
 // copy is a box of whole rows within one page, 128-byte swizzled).  Four warps
-// share 16 rows: each owns 16 keys of every tile, with its own running max, sum
+// share 16 rows: each owns 16 keys of every tile, with its own running shift, sum
 // and O, so nothing is exchanged until the item's end: S = Q K^T with Q from shared
 // memory, the softmax on S's registers, which are then P's registers for P V.  At
 // the item's end the four states are merged through shared memory.  32 rows take
@@ -54,7 +54,6 @@ template <int NG> constexpr int kStages = NG == 1 ? 2 : 4;
 template <int NG> constexpr int kBlocksPerSm = NG == 1 ? 2 : 1;
 template <int NG> constexpr int kThreads = NG * kGroupThreads + 32;
 constexpr int kItemCost = 1;   // beginning and ending an item, in tiles' time
-constexpr float kShiftSlack = 8.f;  // log2 units: the shift moves when a tile's max exceeds it by this
 
 template <int D, int NG>
 struct Layout {
@@ -83,7 +82,7 @@ struct RowsParams {
     const uint16_t *q;
     int64_t q_token, q_head;
     int4 *records;    // per block: the cut item that begins in it {sequence or -1, row block, kv head, last block}
-    float2 *states;   // per part and row: (max, sum), the max in log2 units
+    float2 *states;   // per part and row: (shift, sum), the shift in log2 units
     float *parts;     // per part: kRows x D
     uint32_t wait_ns;
 };
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
         const int kept_all = kept_keys(g, s, (int)((int64_t)at.rb * kRows / g.group));
         group_barrier(group);
 
-        float o[D / 8][4], top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        float o[D / 8][4], shift[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
 #pragma unroll
@@ -337,17 +336,18 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * g.kscale;
                 scale[e] = 1.f;
-                if (mx > top[e] + kShiftSlack) {
-                    scale[e] = ex2(top[e] - mx);  // 0 from -inf
-                    top[e] = mx;
+                if (mx > shift[e] + (kShiftBelow<T> + kShiftSlack)) {
+                    const float to = mx - kShiftBelow<T>;
+                    scale[e] = ex2(shift[e] - to);  // 0 from -inf
+                    shift[e] = to;
                     sum[e] *= scale[e];
                     moved = true;
                 }
-                const float shift = safe_shift(top[e]);
-                const float p0 = ex2(fmaf(x[0][2 * e], g.kscale, -shift));
-                const float p1 = ex2(fmaf(x[0][2 * e + 1], g.kscale, -shift));
-                const float p2 = ex2(fmaf(x[1][2 * e], g.kscale, -shift));
-                const float p3 = ex2(fmaf(x[1][2 * e + 1], g.kscale, -shift));
+                const float below = safe_shift(shift[e]);
+                const float p0 = ex2(fmaf(x[0][2 * e], g.kscale, -below));
+                const float p1 = ex2(fmaf(x[0][2 * e + 1], g.kscale, -below));
+                const float p2 = ex2(fmaf(x[1][2 * e], g.kscale, -below));
+                const float p3 = ex2(fmaf(x[1][2 * e + 1], g.kscale, -below));
                 sum[e] += (p0 + p1) + (p2 + p3);
                 pf[e] = pack2<T>(p0, p1);
                 pf[2 + e] = pack2<T>(p2, p3);
@@ -406,13 +406,13 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
             float l = sum[e];
             l += __shfl_xor_sync(0xffffffffu, l, 1);
             l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if ((lane & 3) == 0) merge_state[slice * 16 + 8 * e + (lane >> 2)] = make_float2(top[e], l);
+            if ((lane & 3) == 0) merge_state[slice * 16 + 8 * e + (lane >> 2)] = make_float2(shift[e], l);
         }
         const bool whole = piece.whole();
         const int64_t part = piece.part();
         static_assert(16 * L::kCols / 4 == kGroupThreads, "four columns of a row to each thread");
         const int r = tid / (L::kCols / 4), c4 = tid % (L::kCols / 4) * 4;
-        float weight[kWarps], all = 0.f, shift = -INFINITY;
+        float weight[kWarps], all = 0.f, common = -INFINITY;
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += L::kCols) {
             group_barrier(group);  // Q (or the previous columns) has been read
@@ -426,11 +426,11 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
             group_barrier(group);
             if (c0 == 0) {
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) shift = fmaxf(shift, merge_state[w * 16 + r].x);
+                for (int w = 0; w < kWarps; ++w) common = fmaxf(common, merge_state[w * 16 + r].x);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 st = merge_state[w * 16 + r];
-                    weight[w] = ex2(st.x - safe_shift(shift));
+                    weight[w] = ex2(st.x - safe_shift(common));
                     all += st.y * weight[w];
                 }
             }
@@ -452,11 +452,11 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
                     w.x = pack2<T>(acc.x * inv, acc.y * inv);
                     w.y = pack2<T>(acc.z * inv, acc.w * inv);
                     *reinterpret_cast<uint2 *>(g.o + token * g.o_token + head * g.o_head + c0 + c4) = w;
-                    if (g.lse && c0 == 0 && c4 == 0) g.lse[token * g.heads + head] = natural_lse(shift, all);
+                    if (g.lse && c0 == 0 && c4 == 0) g.lse[token * g.heads + head] = natural_lse(common, all);
                 } else {
                     const int64_t row = part * kRows + 16 * group + r;
                     *reinterpret_cast<float4 *>(p.parts + row * D + c0 + c4) = acc;
-                    if (c0 == 0 && c4 == 0) p.states[row] = make_float2(shift, all);
+                    if (c0 == 0 && c4 == 0) p.states[row] = make_float2(common, all);
                 }
             }
         }

@@ -6,7 +6,7 @@
 // `group` heads, so K and V are loaded once for the whole group and the last,
 // partly masked tiles are narrow in tokens.  Keys go by in tiles of 128:
 //     S_t = Q_t K^T (TMEM)  ->  P_t = 2^(S_t k - m)  (TMEM, 16 bits)  ->  O_t += P_t V (TMEM)
-// with the running max m and sum l of a row in its thread's registers, and
+// with the running shift m and sum l of a row in its thread's registers, and
 // O_t / l written once.  The arithmetic is the dense kernel's (k_attention.cu:
 // lazy shift, packed fp32 pairs).  What bounds it is the tensor pipe (78 % active
 // on 8192 tokens of 32/8 heads of 128, 644 us or 1706 TFLOP/s without a mask): a
@@ -60,7 +60,6 @@ constexpr int kItemCost = 2;   // beginning and ending an item, in tiles' time (
 // Key tiles of an item that hold keys some row of it does not keep: its rows'
 // kept keys end within 256 tokens of each other.
 constexpr int kEdgeTiles = 3;
-constexpr float kShiftSlack = 8.f;  // log2 units: the shift moves when a tile's max exceeds it by this
 
 template <int D>
 struct Layout {
@@ -597,10 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m_tile = max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * g.kscale;
                 float alpha = 1.f;
                 bool moved = false;
-                if (m_tile > m_run + kShiftSlack) {
-                    alpha = ex2(m_run - m_tile);  // 0 on the first tile with keys
+                if (m_tile > m_run + (kShiftBelow<T> + kShiftSlack)) {
+                    const float to = m_tile - kShiftBelow<T>;
+                    alpha = ex2(m_run - to);  // 0 on the first tile with keys
                     l_run *= alpha;
-                    m_run = m_tile;
+                    m_run = to;
                     moved = j > 0;
                 }
                 const float shift = safe_shift(m_run);

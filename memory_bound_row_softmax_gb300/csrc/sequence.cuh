@@ -279,10 +279,19 @@ __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity, volat
     atomicOr(error_word, kErrWaitTimeout);
 }
 
-// The logarithm of a row's sum from its (max, sum) state: the max in log2
+// How far a row's shift lies below the max that set it, in log2 units: a key of score x
+// weighs P = 2^(x k - shift), rounded to the type for the second product.  fp16 loses
+// bits below 2^-14 and everything below 2^-25, while many such keys (131000 of 2^-25
+// beside one of 1: 0.004 of the row) count in the fp32 sum; with the max at 2^7, and at
+// 2^15 where the shift lags behind by kShiftSlack, nothing is lost above 2^-32.  bf16
+// has the range of fp32.
+constexpr float kShiftSlack = 8.f;  // log2 units: the shift moves when a tile's max exceeds its own by this
+template <typename T> constexpr float kShiftBelow = std::is_same<T, __half>::value ? 7.f : 0.f;
+
+// The logarithm of a row's sum from its (shift, sum) state: the shift in log2
 // units, the sum relative to it.
-__device__ __forceinline__ float natural_lse(float top, float sum) {
-    return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+__device__ __forceinline__ float natural_lse(float shift, float sum) {
+    return sum == 0.f ? -INFINITY : (shift + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b) { return Elem<T>::unpair(a, b); }
