@@ -1033,4 +1033,5 @@ int softmax_abi_version(void) { return kAbiVersion; }
 namespace mbrs {
 int host_device_sms(int *sms) { return device_sms(sms); }
 int64_t host_wait_ns() { return g_wait_ns.load(); }
+int host_launch_overlap() { return g_overlap.load(); }
 }  // namespace mbrs

@@ -173,21 +173,21 @@ __global__ void __launch_bounds__(kThreads) k_cache_append(const Params p) {
 }
 
 template <typename T, int D, bool INTERLEAVED>
-cudaError_t go(const Params &p, int64_t tokens, cudaStream_t stream) {
+cudaError_t go(const Params &p, int64_t tokens, int overlap, cudaStream_t stream) {
     LaunchArgs l = {};
     l.stream = stream;
-    l.overlap = 1;
+    l.overlap = overlap;
     return launch_kernel(k_cache_append<T, D, INTERLEAVED>, l, tokens, kThreads, 0, 0, p);
 }
 
 template <typename T, int D>
-cudaError_t go_pairs(const Params &p, int64_t tokens, bool interleaved, cudaStream_t stream) {
-    return interleaved ? go<T, D, true>(p, tokens, stream) : go<T, D, false>(p, tokens, stream);
+cudaError_t go_pairs(const Params &p, int64_t tokens, bool interleaved, int overlap, cudaStream_t stream) {
+    return interleaved ? go<T, D, true>(p, tokens, overlap, stream) : go<T, D, false>(p, tokens, overlap, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_append(const softmax_append_args_t &a, cudaStream_t stream) {
+cudaError_t launch_append(const softmax_append_args_t &a, int overlap, cudaStream_t stream) {
     Params p;
     p.k = (const uint16_t *)a.k;
     p.v = (const uint16_t *)a.v;
@@ -211,10 +211,10 @@ cudaError_t launch_append(const softmax_append_args_t &a, cudaStream_t stream) {
     p.half = a.inv_freq ? (int)(a.rotary_dim / 2) : 0;
     const bool il = a.interleaved != 0;
     if (a.dtype == SOFTMAX_BF16)
-        return a.head_dim == 128 ? go_pairs<__nv_bfloat16, 128>(p, a.tokens, il, stream)
-                                 : go_pairs<__nv_bfloat16, 64>(p, a.tokens, il, stream);
-    return a.head_dim == 128 ? go_pairs<__half, 128>(p, a.tokens, il, stream)
-                             : go_pairs<__half, 64>(p, a.tokens, il, stream);
+        return a.head_dim == 128 ? go_pairs<__nv_bfloat16, 128>(p, a.tokens, il, overlap, stream)
+                                 : go_pairs<__nv_bfloat16, 64>(p, a.tokens, il, overlap, stream);
+    return a.head_dim == 128 ? go_pairs<__half, 128>(p, a.tokens, il, overlap, stream)
+                             : go_pairs<__half, 64>(p, a.tokens, il, overlap, stream);
 }
 
 }  // namespace seq

@@ -588,10 +588,10 @@ cudaError_t go(const AttnCall &c) {
     const int64_t join_rows = std::min<int64_t>((rows + c.a.batch - 1) / c.a.batch, 8 * NG);
     LaunchArgs l = {};
     l.stream = c.stream;
-    l.overlap = 1;
+    l.overlap = c.overlap;
     e = launch_kernel(k_seq_rows<T, D, NG>, l, blocks, kThreads<NG>, L::kBytes, 0, tk, tv, p);
     if (e != cudaSuccess) return e;
-    return launch_kernel_2d(k_rows_join<T, D, NG>, c.stream, dim3((unsigned)blocks, (unsigned)join_rows), kJoinWarps * 32, p);
+    return launch_kernel_2d(k_rows_join<T, D, NG>, c, dim3((unsigned)blocks, (unsigned)join_rows), kJoinWarps * 32, p);
 }
 
 template <typename T, int D>

@@ -936,7 +936,7 @@ cudaError_t go(const AttnCall &c) {
     p.starve = c.starve;
     LaunchArgs l = {};
     l.stream = c.stream;
-    l.overlap = 1;
+    l.overlap = c.overlap;
     if (plan) {
         PlanParams q;
         q.g = p.g;
@@ -958,7 +958,7 @@ cudaError_t go(const AttnCall &c) {
     const int64_t blocks = plan ? c.sms : blocks_with_work(p.g, most_blocks(a), kTile, kItemCost, c.sms);
     e = launch_kernel(k_seq_tiles<T, D>, l, blocks, kThreads, L::kBytes, 0, tq, tk, tv, p);
     if (e != cudaSuccess) return e;
-    return launch_kernel_2d(k_tiles_join<T, D>, c.stream, dim3((unsigned)blocks, 2 * D / 16), kTile, p);
+    return launch_kernel_2d(k_tiles_join<T, D>, c, dim3((unsigned)blocks, 2 * D / 16), kTile, p);
 }
 
 }  // namespace

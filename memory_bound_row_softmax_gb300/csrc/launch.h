@@ -151,8 +151,10 @@ constexpr int kNoAllocThreads = 256, kNoAllocVpt = 4;
 cudaError_t launch_split_noalloc(const LaunchArgs &a, int64_t chunks, int64_t chunk_vecs, int64_t grid);
 
 // host state of the softmax ABI that the attention ABI (attention_abi.cu)
-// shares: the device's SM count (cached) and the bounded-wait limit
+// and the sequence calls' (sequence_abi.cu) share: the device's SM count
+// (cached), the bounded-wait limit and the launch-overlap switch
 int host_device_sms(int *sms);
 int64_t host_wait_ns();
+int host_launch_overlap();
 
 }  // namespace mbrs

@@ -179,7 +179,8 @@ int attention_call(const softmax_sequence_args_t *args, bool paged, void *worksp
     for (const Span &x : in)
         if (meet(sw, x)) return SOFTMAX_ERR_OVERLAP;
     if (meet(sw, so) || (a.lse && meet(sw, sl))) return SOFTMAX_ERR_OVERLAP;
-    const seq::AttnCall call{a, paged, workspace, sms, host_wait_ns(), attn::attention_starve(), stream};
+    const seq::AttnCall call{a, paged, workspace, sms, host_wait_ns(), attn::attention_starve(),
+                             host_launch_overlap(), stream};
     const cudaError_t e = few_rows(a) ? seq::launch_rows(call) : seq::launch_tiles(call);
     return e == cudaSuccess ? SOFTMAX_OK : SOFTMAX_ERR_CUDA;
 }
@@ -277,7 +278,7 @@ int softmax_kv_cache_append(const softmax_append_args_t *args, cudaStream_t stre
                               (a.heads == 1 || a.q_head_stride == a.q_out_head_stride);
         if (!in_place && views_meet(q, o)) return SOFTMAX_ERR_OVERLAP;
     }
-    return seq::launch_append(a, stream) == cudaSuccess ? SOFTMAX_OK : SOFTMAX_ERR_CUDA;
+    return seq::launch_append(a, host_launch_overlap(), stream) == cudaSuccess ? SOFTMAX_OK : SOFTMAX_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -113,18 +113,18 @@ inline cudaError_t opt_in_shared_memory(const void *kernel, int bytes, std::atom
     return e;
 }
 
-// launch_kernel with a two-dimensional grid, allowed to be scheduled early.
+// launch_kernel with a two-dimensional grid, on the call's stream.
 template <typename... P, typename... A>
-cudaError_t launch_kernel_2d(void (*kernel)(P...), cudaStream_t stream, dim3 grid, int threads, A &&...args) {
+cudaError_t launch_kernel_2d(void (*kernel)(P...), const AttnCall &c, dim3 grid, int threads, A &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.stream = stream;
+    cfg.stream = c.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = c.overlap ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -10,8 +10,9 @@
 namespace mbrs {
 namespace seq {
 
-// Checked by the ABI: sizes, strides, alignment, overlaps.
-cudaError_t launch_append(const softmax_append_args_t &a, cudaStream_t stream);
+// Checked by the ABI: sizes, strides, alignment, overlaps.  overlap, here and
+// below: softmax_set_launch_overlap's setting.
+cudaError_t launch_append(const softmax_append_args_t &a, int overlap, cudaStream_t stream);
 
 // Attention.  Both launchers take the workspace the ABI has checked against
 // the bytes below.
@@ -22,6 +23,7 @@ struct AttnCall {
     int sms;
     int64_t wait_ns;
     int starve;  // a test hook (softmax_attention_set_wait_test)
+    int overlap;
     cudaStream_t stream;
 };
 
