@@ -108,9 +108,10 @@ int softmax_attention_plan(int64_t batch, int64_t heads, int64_t n_ctx, int64_t 
                            int num_sms, softmax_attention_plan_t *plan);
 
 /*
- * Test hook for the attention forward's bounded waits.  starve != 0 makes the
- * next launches leave every block's first Q barrier unarmed, so that wait can
- * only run out: the kernel records SOFTMAX_ERR_TIMEOUT (read it with
+ * Test hook for the bounded waits of the attention forward and of the sequence
+ * attention calls (mbrs_sequence.h).  starve != 0 makes the next launches leave
+ * every block's first Q barrier (of few query rows: its first key tile's)
+ * unarmed, so that wait can only run out: the kernel records SOFTMAX_ERR_TIMEOUT (read it with
  * softmax_check_device_error), skips its stores and returns normally.  The
  * wait limit is the one softmax_set_wait_test sets (default 1 s).
  * Process-wide, not thread-safe; returns SOFTMAX_OK.

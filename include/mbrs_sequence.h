@@ -74,7 +74,8 @@
  *   SOFTMAX_ERR_CUDA        a CUDA call or launch failed
  * A call with no rows (tokens == 0 or batch == 0) returns SOFTMAX_OK without a
  * launch.  A bounded wait inside a kernel that runs out is reported by
- * softmax_check_device_error as SOFTMAX_ERR_TIMEOUT.
+ * softmax_check_device_error as SOFTMAX_ERR_TIMEOUT; what that call leaves in o
+ * and lse is undefined.
  */
 #ifndef MBRS_SEQUENCE_H
 #define MBRS_SEQUENCE_H

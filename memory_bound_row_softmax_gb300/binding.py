@@ -667,8 +667,8 @@ def attention_plan(batch: int, heads: int, n_ctx: int, head_dim: int = 128, dtyp
 
 
 def set_attention_wait_test(starve: bool = False) -> None:
-    """Attention forward test hook: leave the first Q barrier of every block
-    unarmed so that its bounded wait runs out (see set_wait_test for the limit)."""
+    """Test hook of the attention calls: leave the first Q barrier (or key tile's) of
+    every block unarmed so that its bounded wait runs out (see set_wait_test for the limit)."""
     lib().softmax_attention_set_wait_test(1 if starve else 0)
 
 

@@ -85,6 +85,7 @@ struct RowsParams {
     float2 *states;   // per part and row: (shift, sum), the shift in log2 units
     float *parts;     // per part: kRows x D
     uint32_t wait_ns;
+    int starve;       // test hook: leave the first tile's barrier unarmed
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t *r) {
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
                     ok = wait_phase(empty(stage), ((n / kStages) - 1) & 1, abort_flag, &g_rows_error, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                if (p.starve && n == 0) continue;  // the test hook: this tile never lands
                 const uint32_t copies = (uint32_t)__popc(__ballot_sync(0xffffffffu, live));
                 if (lane == 0) {
                     if (copies) mbar_arrive_expect_tx(full(stage), copies * box_bytes);
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
         }
         // every copy issued lands before the block may exit
         if (lane == 0)
-            for (int m = n > kStages ? n - kStages : 0; m < n; ++m)
+            for (int m = n > kStages ? n - kStages : p.starve ? 1 : 0; m < n; ++m)
                 drain_phase(full(m % kStages), (m / kStages) & 1, abort_flag, &g_rows_error, p.wait_ns);
         return;
     }
@@ -413,6 +415,7 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
         static_assert(16 * L::kCols / 4 == kGroupThreads, "four columns of a row to each thread");
         const int r = tid / (L::kCols / 4), c4 = tid % (L::kCols / 4) * 4;
         float weight[kWarps], all = 0.f, common = -INFINITY;
+        bool good = ok;  // and every other warp of the group has had its tiles
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += L::kCols) {
             group_barrier(group);  // Q (or the previous columns) has been read
@@ -425,6 +428,7 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
                         make_float2(o[c0 / 8 + c][2 * e], o[c0 / 8 + c][2 * e + 1]);
             group_barrier(group);
             if (c0 == 0) {
+                good = ok && !*abort_flag;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) common = fmaxf(common, merge_state[w * 16 + r].x);
 #pragma unroll
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
                 acc.x += v.x * weight[w], acc.y += v.y * weight[w];
                 acc.z += v.z * weight[w], acc.w += v.w * weight[w];
             }
-            if (r < rows && ok) {
+            if (r < rows && good) {
                 if (whole) {
                     const int64_t row = row0 + r;
                     const int64_t token = s.start + row / g.group, head = (int64_t)at.h * g.group + row % g.group;
@@ -460,14 +464,14 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
                 }
             }
         }
-        if (!whole && piece.t0 == 0 && ok)
+        if (!whole && piece.t0 == 0 && good)
             record = make_int4(at.b, at.rb, at.h, last_block<kItemCost>(piece, at, pos, stretch));
         pos += piece.count;
         left -= piece.count;
         at = next;
         s = next_s;
     }
-    if (threadIdx.x == 0) p.records[blockIdx.x] = record;
+    if (threadIdx.x == 0) p.records[blockIdx.x] = *abort_flag ? make_int4(-1, 0, 0, 0) : record;
 }
 
 // The cut items: block (x, y) merges rows y, y + gridDim.y, ... of the item that
@@ -583,6 +587,7 @@ cudaError_t go(const AttnCall &c) {
     p.states = reinterpret_cast<float2 *>(w + sp.states);
     p.parts = reinterpret_cast<float *>(w + sp.parts);
     p.wait_ns = wait_limit(c.wait_ns);
+    p.starve = c.starve;
     const int64_t rows = c.a.tokens * p.g.group;
     const int64_t blocks = blocks_with_work(p.g, rows / L::kRows + c.a.batch, kKeys, kItemCost, blocks_of(NG, c.sms));
     const int64_t join_rows = std::min<int64_t>((rows + c.a.batch - 1) / c.a.batch, 8 * NG);

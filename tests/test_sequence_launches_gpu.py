@@ -102,3 +102,53 @@ def test_results_with_and_without_overlap():
     finally:
         B.set_launch_overlap(True)
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+# rows of a sequence, keys and head dim: one group of 16 rows and two, each in whole items
+# and cut ones; tiles of head dim 64 (three S buffers) and 128, whole and cut
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,heads,keys", [([1] * 3, 4, 40), ([1], 4, 5000), ([5] * 3, 5, 40), ([5], 5, 5000),
+                                             ([200, 90], 2, 300), ([300], 2, 9000)], ids=str)
+def test_waits_that_run_out(lens, heads, keys, d):
+    """A tile that never lands: the waits give up and report it, the rows are left as they
+    were (nothing is merged from a workspace that nobody wrote), and the next call is right."""
+    page = 8
+    pages = -(-keys // page)
+    kc, vc = normal(1, pages, page, 1, d), normal(2, pages, page, 1, d)
+    q = normal(3, sum(lens), heads, d)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].repeat(len(lens), 1)
+    klen = ints(*[keys] * len(lens))
+    starts = torch.zeros(len(lens) + 1, dtype=torch.int32, device="cuda")
+    starts[1:] = ints(*lens).cumsum(0)
+    space = torch.full((B.sequence_workspace_bytes(q.shape[0], len(lens), heads, 1, d, "bf16", page_size=page, pages=pages,
+                                                   max_pages=pages),), 255, dtype=torch.uint8, device="cuda")
+
+    def call(out, lse):
+        B.attention_paged_fwd(q, kc, vc, table, klen, starts, out=out, lse=lse, workspace=space)
+        torch.cuda.synchronize()
+        return out, lse
+
+    def outputs():
+        return torch.full_like(q, SENTINEL), torch.full(q.shape[:2], SENTINEL, device="cuda")
+
+    out, lse = outputs()
+    B.set_wait_test(20_000_000)
+    B.set_attention_wait_test(True)
+    try:
+        call(out, lse)
+        assert B.check_device_error() == B.ERR_TIMEOUT
+    finally:
+        B.set_attention_wait_test(False)
+        B.set_wait_test(0)
+    assert (out == SENTINEL).all() and (lse == SENTINEL).all()
+    assert B.check_device_error() == B.OK
+    out, lse = call(*outputs())
+    assert B.check_device_error() == B.OK
+    x = torch.einsum("nhd,cd->nhc", q.double(), kc.flatten(0, 1)[:keys, 0].double()) / math.sqrt(d)
+    seen = torch.cat([torch.arange(keys - n, keys, device="cuda") for n in lens])
+    x = torch.where(torch.arange(keys, device="cuda") <= seen[:, None, None], x, -math.inf)
+    want = x.softmax(-1) @ vc.flatten(0, 1)[:keys, 0].double()
+    # P and o each rounded to bf16 (2^-8 of max|v| and of |o|), and 2^-12 for what is in fp32
+    tol = 2.0 ** -8 * (vc.double().abs().max() + want.abs()) + 2.0 ** -12
+    assert ((out.double() - want).abs() <= tol).all()
+    assert ((lse.double() - torch.logsumexp(x, -1)).abs() <= 2.0 ** -12).all()
