@@ -25,7 +25,8 @@ SOURCES = ["abi.cu", "k_warp.cu", "k_warp_whole.cu", "k_cta.cu", "k_cta_whole.cu
            "k_packed.cu", "k_attention.cu", "attention_abi.cu", "k_seq_rows.cu", "k_seq_tiles.cu", "k_cache_append.cu",
            "sequence_abi.cu"]
 HEADERS = ["common.cuh", "kernels.cuh", "launch.h", "warp_launch.cuh", "cta_launch.cuh", "attention.cuh",
-           "attention_launch.h", "sequence.cuh", "sequence_launch.h", "sequence_host.h", "tensor_map.h"]
+           "attention_launch.h", "sequence.cuh", "sequence_launch.h", "sequence_host.h", "sequence_rules.h",
+           "tensor_map.h"]
 PUBLIC_HEADERS = ["mbrs_softmax.h", "mbrs_attention.h", "mbrs_sequence.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -44,7 +45,7 @@ def cuda_home() -> str:
 # their ABI do not depend on them.
 ATTENTION_ONLY = ["k_attention.cu", "attention_abi.cu", "attention.cuh", "attention_launch.h", "mbrs_attention.h",
                   "k_seq_rows.cu", "k_seq_tiles.cu", "k_cache_append.cu", "sequence_abi.cu", "sequence.cuh", "sequence_launch.h",
-                  "sequence_host.h", "tensor_map.h", "mbrs_sequence.h"]
+                  "sequence_host.h", "sequence_rules.h", "tensor_map.h", "mbrs_sequence.h"]
 
 
 def sources_digest() -> str:

@@ -42,6 +42,7 @@
 #include "launch.h"
 #include "sequence.cuh"
 #include "sequence_host.h"
+#include "sequence_rules.h"
 
 namespace mbrs {
 namespace seq {
@@ -752,13 +753,13 @@ struct PlanParams {
 };
 __global__ void __launch_bounds__(1024) k_tiles_plan(const __grid_constant__ PlanParams p) {
     __shared__ unsigned int bins[kBins], warp_sum[32];
-    __shared__ unsigned long long total;
+    __shared__ unsigned long long total, total_blocks;
     __shared__ int most, least;
     const Geometry &g = p.g;
     pdl_enter();
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
     bins[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) total = 0ull, most = 0, least = 0x7fffffff;
+    if (threadIdx.x == 0) total = 0ull, total_blocks = 0ull, most = 0, least = 0x7fffffff;
     __syncthreads();
     const auto walk = [&](auto &&each) {
         for (int64_t b0 = warp; b0 < g.batch; b0 += 32 * 32) {
@@ -774,21 +775,24 @@ __global__ void __launch_bounds__(1024) k_tiles_plan(const __grid_constant__ Pla
             }
         }
     };
-    unsigned long long own = 0;
+    unsigned long long own = 0, blocks = 0;
     int top = 0, low = 0x7fffffff;
     walk([&](int, int, const Sequence &, int tiles) {
         own += (unsigned long long)tiles;
+        ++blocks;
         top = max(top, tiles);
         low = min(low, tiles);
         atomicAdd(&bins[kBins - 1 - min(tiles >> p.shift, kBins - 1)], 1u);
     });
     for (int o = 16; o; o >>= 1) {
         own += __shfl_xor_sync(0xffffffffu, own, o);
+        blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
     }
     if (lane == 0 && own) {
         atomicAdd(&total, own);
+        atomicAdd(&total_blocks, blocks);
         atomicMax(&most, top);
         atomicMin(&least, low);
     }
@@ -807,14 +811,10 @@ __global__ void __launch_bounds__(1024) k_tiles_plan(const __grid_constant__ Pla
         all += warp_sum[w];
     }
     bins[threadIdx.x] = upto - mine;
-    // Cut where one item is longer than an SM's share, or where the last wave of
-    // items would leave SMs idle for longer than cutting costs: items of one length
-    // leave (waves rounded up - waves) items' time, others at least that of the
-    // shortest (which come last).
-    const unsigned long long items = (unsigned long long)all * (unsigned)g.kv_heads, sms = (unsigned)p.sms;
-    const unsigned long long idle = ((items + sms - 1) / sms * sms - items) * (unsigned)least;
-    const bool cut = (unsigned long long)most * sms > total * (unsigned)g.kv_heads || idle > p.cut_cost * sms ||
-                     all > (unsigned)p.capacity;
+    // (a plan that does not cut has at most `capacity` row blocks: its bins and `all`, in
+    // 32 bits, are exact)
+    const PlanCounts counts{total_blocks, total, (uint32_t)most, (uint32_t)least};
+    const bool cut = plan_cuts(counts, (uint32_t)g.kv_heads, (uint32_t)p.sms, (uint32_t)p.capacity, p.cut_cost);
     if (threadIdx.x == 0) {
         p.plan[0] = 0u;
         p.plan[1] = all * (unsigned)g.kv_heads;
