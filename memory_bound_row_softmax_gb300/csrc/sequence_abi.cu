@@ -9,6 +9,7 @@
 #include "launch.h"
 #include "mbrs_sequence.h"
 #include "sequence_launch.h"
+#include "sequence_rules.h"
 
 using namespace mbrs;
 
@@ -123,13 +124,7 @@ int check_sizes(const softmax_sequence_args_t &a, bool paged) {
     return paged ? check_pages(a.pages, a.page_size, a.max_pages) : SOFTMAX_OK;
 }
 
-// Few query rows to an average sequence and kv head: the kernel that lets the
-// keys stream by; more: the tensor-core tiles.  Measured in us, streaming (one or
-// two groups of 16 rows; four for 33 rows and more) against tiles: 16 x 5 tokens
-// over 2000 keys, 20 rows, 40 and 43; 32 x 4 over 4000 keys, 32 rows, 106 and 119;
-// 16 x 5 over 2000 keys, 40 rows, 27 and 18; 8 x 16 over 4000 keys, 64 rows, 75 and
-// 38.  A batch of both kinds (a chunk beside single tokens) goes by its average.
-bool few_rows(const softmax_sequence_args_t &a) { return a.tokens * (a.heads / a.kv_heads) <= 32 * a.batch; }
+bool few_rows(const softmax_sequence_args_t &a) { return seq::few_rows(a.tokens, a.batch, a.heads / a.kv_heads); }
 
 int64_t workspace_bytes_of(const softmax_sequence_args_t &a, int sms) {
     return few_rows(a) ? seq::rows_workspace_bytes(a, sms) : seq::tiles_workspace_bytes(a, sms);

@@ -14,6 +14,7 @@ extern "C" int plan_cuts_c(uint64_t blocks, uint64_t tiles, uint32_t most, uint3
                            uint32_t capacity, uint32_t cut_cost) {
     return plan_cuts(PlanCounts{blocks, tiles, most, least}, kv_heads, sms, capacity, cut_cost);
 }
+extern "C" int few_rows_c(int64_t tokens, int64_t batch, int64_t group) { return few_rows(tokens, batch, group); }
 """
 
 
@@ -25,6 +26,7 @@ def rules(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I", CSRC, "-o", str(so), str(src)], check=True)
     lib = ctypes.CDLL(str(so))
     u32, u64 = ctypes.c_uint32, ctypes.c_uint64
+    lib.few_rows_c.argtypes = [ctypes.c_int64] * 3
     lib.plan_cuts_c.argtypes = [u64, u64] + [u32] * 6
     return lib
 
@@ -45,3 +47,21 @@ def test_cutting(rules):
     assert rules.plan_cuts_c(100, 100 + 200, 200, 1, 8, 152, 1000, 14)
     # nothing to do
     assert not rules.plan_cuts_c(0, 0, 0, 2**31 - 1, 8, 152, 1000, 14)
+
+
+def test_which_kernel(rules):
+    few = rules.few_rows_c
+    # single tokens and drafts, whatever their number
+    for batch in (1, 64, 5000):
+        for group in (1, 4, 8, 16):
+            assert few(batch, batch, group)
+    assert few(128 * 4, 128, 4) and few(32 * 4, 32, 8) and few(48 * 6, 48, 4) and few(5, 1, 5)
+    # many rows a sequence
+    assert not few(300, 1, 1) and not few(16 * 5, 16, 8) and not few(512, 1, 4)
+    # a low average of a few long sequences and many of one token, or of none
+    assert not few(448 + 64, 65, 4) and not few(900 + 128, 129, 4) and not few(97 + 190, 191, 16)
+    assert not few(2000, 256, 4) and not few(16000, 2000, 4)
+    # padding rows count like tokens of no sequence
+    assert few(64 + 13, 64, 8)
+    # sizes at the index range
+    assert few(2**31 - 1025, 2**31 - 1025, 16) and not few(2**31 - 1025, 1, 128)
