@@ -36,8 +36,9 @@
  * Values read on the device (q_starts, kv_lens, page_table) cannot be checked
  * before the launch.  Whatever they hold, no call reads or writes outside the
  * buffers it was given: q_starts are clamped to [0, tokens] and a sequence that
- * ends before it starts is empty; kv_lens are clamped to [0, max_pages *
- * page_size].  They may change between launches (and between the replays of a
+ * ends before it starts is empty; attention clamps kv_lens to [0, max_pages *
+ * page_size], and the append, which takes positions from them as they are, drops
+ * the keys and values of positions that have no page.  They may change between launches (and between the replays of a
  * captured graph) with the sizes below kept.
  *
  * Types: SOFTMAX_F16 or SOFTMAX_BF16; head_dim 64 or 128; heads a multiple of
@@ -154,7 +155,8 @@ typedef struct {
  * the angle reduced in 64 bits, the rotation in fp32, rounded once; elements
  * from rotary_dim on are copied.  A token whose position is negative or has no
  * page in [0, pages) writes no cache (its query is rotated all the same).  Two
- * tokens of one call on the same slot leave either's row there.
+ * tokens of one call on the same slot leave elements of either there, in pieces
+ * of 8.
  */
 int softmax_kv_cache_append(const softmax_append_args_t *args, cudaStream_t stream);
 
