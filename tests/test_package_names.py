@@ -12,6 +12,15 @@ def test_a_replaced_function_is_reached_through_the_package(monkeypatch):
     assert pkg.status_string is first
 
 
+def test_a_function_set_in_the_package_stays(monkeypatch):
+    def mine(status):
+        return "mine"
+    pkg.status_string
+    monkeypatch.setattr(pkg, "status_string", mine)
+    monkeypatch.setattr(binding, "status_string", lambda status: "replaced")
+    assert pkg.status_string is mine
+
+
 def test_names():
     for name in pkg._BINDING_NAMES:
         assert getattr(pkg, name) is getattr(binding, name)
