@@ -5,17 +5,18 @@
 // heads that share one key/value head (row r: token r / group, head r % group),
 // 16 or 32 of them; its keys go by in tiles of 64.  With so few rows every
 // K and V byte is used once, so HBM bounds the call (64 tokens over 37 to 8000
-// keys, 988 MB, 160 us: 6.17 TB/s, 0.91 of a copy's rate), and the products need far
-// less than the tensor cores have: 16-row mma.sync tiles, whose accumulators are
+// keys, 988 MB, 159-165 us: 6.0-6.2 TB/s, 0.88-0.91 of a copy's rate), and the products
+// need far less than the tensor cores have: 16-row mma.sync tiles, whose accumulators are
 // registers, keep the warps independent of each other (a 128-row tcgen05 tile
 // would be seven eighths empty).
 //
 // Work split: the work of all items, in the order (sequence, row block, kv head),
-// is cut into equal stretches, one per block, whatever the sequences' lengths.  Each block finds its stretch from q_starts and kv_lens
-// itself (one scan over the batch).  A block walks its stretch item by item; an
-// item it holds whole is finished there, of a cut one the part's (shift, sum, O)
-// goes to the workspace in fp32 and k_rows_join merges the parts in order
-// (the merge rule of common.cuh), so results do not depend on timing.
+// is cut into equal stretches, one per block, whatever the sequences' lengths.  Each
+// block finds its stretch from q_starts and kv_lens itself (one scan over the batch).
+// A block walks its stretch item by item; an item it holds whole is finished there, of
+// a cut one the part's (shift, sum, O) goes to the workspace in fp32 and k_rows_join
+// merges the parts in order (the merge rule of common.cuh), so results do not depend on
+// timing.
 //
 // Roles: the last warp feeds a ring of K/V tiles with TMA (one lane per copy: a
 // copy is a box of whole rows within one page, 128-byte swizzled).  Four warps
@@ -482,7 +483,8 @@ __global__ void __launch_bounds__(kThreads<NG>, kBlocksPerSm<NG>)
 // (gridDim.y: the rows of an average item, at most 8 of each row group.  8 instead of
 // 4: five tokens of 40/8 heads, 25 rows, 3394 keys, 22.8 -> 14.1 us; 14970 keys of
 // one head, 27.2 -> 22.7; 16 where items have few rows are blocks for nothing, 10.6 ->
-// 12.8 for one token of 32/8 heads.)
+// 12.8 for one token of 32/8 heads.  What it costs: items that are not cut get their
+// blocks all the same, 9.7 -> 11.7 for 14 prompts of 18 rows on average.)
 constexpr int kJoinWarps = 8;
 template <typename T, int D, int NG>
 __global__ void __launch_bounds__(kJoinWarps * 32) k_rows_join(const __grid_constant__ RowsParams p) {

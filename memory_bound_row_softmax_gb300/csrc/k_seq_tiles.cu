@@ -9,13 +9,15 @@
 // with the running shift m and sum l of a row in its thread's registers, and
 // O_t / l written once.  The arithmetic is the dense kernel's (k_attention.cu:
 // lazy shift, packed fp32 pairs).  What bounds it is the tensor pipe (78 % active
-// on 8192 tokens of 32/8 heads of 128, 644 us or 1706 TFLOP/s without a mask): a
-// pair of tiles takes 2600 cycles, 2048 of them products, and each group's softmax,
-// 1110 between its S and its P, hides behind the other's products.  With head dim
-// 64 the products are half and the softmax groups and the thread that issues the
-// products are what is left: three S buffers, and one wait per tile landed, take
-// 4 x 2048 tokens of 16 heads of 64 from 89.7 to 82.5 us (833 TFLOP/s), and from
-// 59.7 to 55.1 us with the causal mask.
+// on 8192 tokens of 32/8 heads of 128 without a mask: 619 us under the profiler, at
+// 1.90 GHz, 629-644 us or 1707-1748 TFLOP/s in calls): a pair of tiles takes 2600
+// cycles, 2048 of them products, and each group's softmax, 1110 between its S and its
+// P, hides behind the other's products.  With head dim 64 the products are half, 1024
+// a pair of tiles, and the thread that issues them is what is left: it serves both
+// groups, 1100 cycles a tile and so 2200 a pair, where the groups' softmax, side by
+// side, takes 1200.  Three S buffers, and one wait per tile landed, took 4 x 2048
+// tokens of 16 heads of 64 from 89.7 to 82.5 us (833 TFLOP/s; 78-80 on another box),
+// and from 59.7 to 55.1 us with the causal mask.
 //
 // Threads: warps 0-3 and 4-7 are the softmax groups of tiles A and B (thread r
 // = row r = TMEM lane r); warp 8 fetches work and feeds TMA, one lane per copy
@@ -57,7 +59,7 @@ constexpr int kTile = 128;     // rows of a query tile, keys of a key tile
 constexpr int kThreads = 320;
 constexpr int kWarpTma = 8, kWarpMma = 9;
 constexpr int kItemsPerSm = 2;
-constexpr int kItemCost = 2;   // beginning and ending an item, in tiles' time (3 us of 1.6 us each)
+constexpr int kItemCost = 2;   // beginning and ending an item, in tiles' time (about 2.4 us of 1.4 us each)
 // Key tiles of an item that hold keys some row of it does not keep: its rows'
 // kept keys end within 256 tokens of each other.
 constexpr int kEdgeTiles = 3;
