@@ -16,7 +16,7 @@
 // a pair of tiles, and the thread that issues them is what is left: it serves both
 // groups, 1100 cycles a tile and so 2200 a pair, where the groups' softmax, side by
 // side, takes 1200.  Three S buffers, and one wait per tile landed, took 4 x 2048
-// tokens of 16 heads of 64 from 89.7 to 82.5 us (833 TFLOP/s; 78-80 on another box),
+// tokens of 16 heads of 64 from 89.7 to 82.5 us (833 TFLOP/s; 78-80 on another GB300),
 // and from 59.7 to 55.1 us with the causal mask.
 //
 // Threads: warps 0-3 and 4-7 are the softmax groups of tiles A and B (thread r
